@@ -192,8 +192,10 @@ struct Tile {
   float us, us_k, more, more_k;
 };
 
+int64_t tile_count(const Tile& t, int64_t M, int64_t N) { return ((M + t.rows - 1) / t.rows) * ((N + t.cols - 1) / t.cols); }
+
 float tile_us(const Tile& t, int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = ((M + t.rows - 1) / t.rows) * ((N + t.cols - 1) / t.cols), rounds = (tiles + 255) / 256;
+  const int64_t rounds = (tile_count(t, M, N) + 255) / 256;
   const float k = (float)K / 1024.0f;
   return t.us + t.us_k * k + (float)(rounds - 1) * (t.more + t.more_k * k);
 }
@@ -297,9 +299,20 @@ bool pair_launch(const q4::GemmA8Args& a, hipStream_t s) {
 // first saves more than the second costs: 1.5 us and 4 TB/s on the GPU, and a
 // host that needs 9 us for the two launches (16 x 1024 x 8192: 13 us against
 // 52; 4 x 8192 x 2048: 9.3 against 14; 10 x 1152 x 64: 9.6 against 6).
+// Only while the one launch has at most two workgroups per compute unit: past
+// that the chip is full, the two estimates differ by less than their error
+// where K passes the fitted range, and the second launch would have to move
+// M x N float32 values (two launches / one, us: 5474 x 320 x 10944 of 258
+// workgroups 108 / 144, 1226 x 1600 x 10368 of 507 118 / 130; 4096 x 8192 x
+// 28672 of 4096 3429 / 3396, 8192 x 8192 x 20480 of 8192 4907 / 4856). So
+// `work` is at most 512 x 64 x 128 floats, and the quantizer's launch is far
+// inside its limit whenever the pair's has been enqueued.
+constexpr int64_t kSplitTiles = 512;
 bool quant_splits(int64_t M, int64_t N, int64_t K) {
   M = rows16(M);
-  const float whole = tile_us(kPairQuant[best_tile(kPairQuant, M, N, K)], M, N, K);
+  const Tile& t = kPairQuant[best_tile(kPairQuant, M, N, K)];
+  if (tile_count(t, M, N) > kSplitTiles) return false;
+  const float whole = tile_us(t, M, N, K);
   const float parts = tile_us(kPairExact[best_tile(kPairExact, M, N, K)], M, N, K) + 1.5f + (float)(M * N) * 9.0f / 4e6f;
   return whole > (parts > 9.0f ? parts : 9.0f);
 }

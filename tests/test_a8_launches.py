@@ -1,0 +1,47 @@
+"""Which kernels the 8-bit activation calls launch, recorded without a GPU: a
+refused call launches nothing, and the SwiGLU with 8-bit results takes two
+launches and scratch memory only where its one launch would leave compute
+units without work."""
+
+import pytest
+
+import bit_weight_only_q4g64_amd as q4
+from tests.launch_record import available, record
+
+pytestmark = pytest.mark.skipif(not available, reason="needs the ROCm compilers")
+
+
+def test_a_refused_call_launches_nothing():
+    """Sizes around the most lanes a launch may have (2^32), where one of two launches could fit and the other not."""
+    calls = [("quant", 2**24, 2048), ("quant", 2**24, 2**20), ("norm", 2**24, 2048), ("norm", 2**24, 16384)]
+    for m in range(4, 25):
+        for n in range(6, 31):
+            for k in (64, 2048, 16384, 20480, 65536, 2**20):
+                if n + k.bit_length() <= 40:
+                    calls += [("swiglu", 2**m, 2**n, k), ("product", 2**m, 2**n, k, "bf16"), ("pair", 2**m, 2**n, k, "f32")]
+    refused = 0
+    for call, r in zip(calls, record(calls)):
+        assert r.status in (q4.Q4_OK, q4.Q4_EINVAL, q4.Q4_EUNSUPPORTED), call
+        assert (len(r.launches) > 0) == (r.status == q4.Q4_OK), (call, r)
+        assert all(x.workgroups * x.lanes < 2**32 for x in r.launches), (call, r)
+        refused += r.status != q4.Q4_OK
+    assert refused > 100
+
+
+def test_scratch_memory_stays_small():
+    """M x N float32 values of scratch memory for few workgroups only, however long K is (512 of 64 x 128 at most)."""
+    need = q4.a8_swiglu_work_bytes
+    for M, N, K in ((8192, 8192, 20480), (4096, 8192, 28672), (8192, 8192, 65536), (2**18, 2**17, 16384), (2048, 28672, 2**20)):
+        assert need(M, N, K) == 0, (M, N, K)
+    sizes = [(2**m + d, 2**n, k) for m in range(4, 21) for d in (0, 1) for n in range(6, 20) for k in (64, 1024, 8192, 16384, 20480, 2**16, 2**20)]
+    assert max(need(*s) for s in sizes) <= 512 * 64 * 128 * 4
+    # few workgroups still take the two launches
+    for M, N, K in ((16, 1024, 8192), (4, 8192, 2048), (5474, 320, 10944), (1226, 1600, 10368)):
+        assert need(M, N, K) == M * N * 4, (M, N, K)
+
+
+def test_launches_agree_with_the_scratch_memory():
+    calls = [("swiglu", M, N, K) for M in (1, 16, 17, 300, 5474, 8192) for N in (64, 320, 1600, 8192) for K in (64, 2048, 10368, 20480)]
+    for call, r in zip(calls, record(calls)):
+        assert r.status == q4.Q4_OK and len(r.launches) == (2 if r.work_bytes else 1), (call, r)
+        assert r.work_bytes == q4.a8_swiglu_work_bytes(*call[1:]), call
