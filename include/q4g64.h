@@ -435,9 +435,10 @@ float qmv_window_cost(const float* us, int R);
  * aligned with rows that stay so, gamma 16-byte, scales 4-byte aligned with
  * strides of at most 2^24. Codes and scales may hold any bits: a NaN anywhere
  * makes the outputs of its row (of its columns, in a weight) NaN and no
- * others. The norm adds squares in float32: a row whose sum of squares passes
- * the largest float32 gives zeros (NaN where h is infinite), and a row of
- * zeros with eps = 0 gives NaN.
+ * others. The norm adds squares in float32, or in float64 where a row's would
+ * leave float32, so every row of finite values has its norm; a row of zeros
+ * with eps = 0 gives NaN, and one with an infinity NaN there and zeros
+ * elsewhere.
  *
  * Float32 and a8 results are sums of exact products, added in float32. A
  * Q4_BF16 product comes from the 8-bit matrix instructions, up to twice as
