@@ -435,7 +435,11 @@ float qmv_window_cost(const float* us, int R);
  * aligned with rows that stay so, gamma 16-byte, scales 4-byte aligned with
  * strides of at most 2^24. Codes and scales may hold any bits: a NaN anywhere
  * makes the outputs of its row (of its columns, in a weight) NaN and no
- * others. The norm adds squares in float32, or in float64 where a row's would
+ * others, but for an a8 result, where it takes the whole group of 128 columns
+ * that its column lies in, in every row, because they share a scale. (The
+ * scales' product sx * sw is a float32 too: where it overflows, the group's
+ * part of the row is infinite or NaN.)
+ * The norm adds squares in float32, or in float64 where a row's would
  * leave float32, so every row of finite values has its norm; a row of zeros
  * with eps = 0 gives NaN, and one with an infinity NaN there and zeros
  * elsewhere.
