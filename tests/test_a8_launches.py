@@ -3,9 +3,12 @@ refused call launches nothing, and the SwiGLU with 8-bit results takes two
 launches and scratch memory only where its one launch would leave compute
 units without work."""
 
+import re
+
 import pytest
 
 import bit_weight_only_q4g64_amd as q4
+from tests.a8_shapes import PAIRS, PRODUCTS
 from tests.launch_record import available, record
 
 pytestmark = pytest.mark.skipif(not available, reason="needs the ROCm compilers")
@@ -45,3 +48,39 @@ def test_launches_agree_with_the_scratch_memory():
     for call, r in zip(calls, record(calls)):
         assert r.status == q4.Q4_OK and len(r.launches) == (2 if r.work_bytes else 1), (call, r)
         assert r.work_bytes == q4.a8_swiglu_work_bytes(*call[1:]), call
+
+
+def tile_of(kernel):
+    """(rows, columns, the fewest groups of K that turn the loads' ring twice, places the ring can end at) of a product
+    kernel by its template arguments, and whether its weights are loaded past the caches."""
+    kind, args, flags = re.fullmatch(r"q4::a8_(tile|direct)_kernel<q4::\w+<(.*)>, (.*)>", kernel).groups()
+    a = [{"true": 1, "false": 0}.get(v, v) for v in args.split(", ")]
+    if kind == "tile":
+        exact, pair, wm, wn, mt, ns, ahead, _ = map(int, a)
+        return wm * mt * 32, wn * ns * 32 // (1 + pair), 2 * (ahead + 2) + 1, ahead if exact else ahead + 1, flags.endswith("true")
+    _, mt, nt, _, nw, kw, ahead = map(int, a)
+    return mt * 16, nw * nt * 16, kw * (ahead + 1) + 1, 1, False  # kw waves share the groups
+
+
+def test_shapes_take_every_kernel_through_its_pipeline():
+    """Of every kernel that the sizes of a wide grid launch, tests/a8_shapes.py holds sizes with row and column ends inside
+    its tile, half a group at the end of K, and K long enough for two turns of the ring, ending at each of its places."""
+    grid = [(M, N, K) for M in (1, 17, 33, 64, 100, 128, 200, 300, 520, 1000, 2000, 4000, 8192) for N in (64, 256, 1024, 2048, 4096, 16384, 65536)
+            for K in (64, 256, 1024, 2048, 8192)]
+    forms = [("product", "f32"), ("product", "bf16"), ("pair", "f32"), ("pair", "bf16"), ("swiglu", "")]
+
+    def kernels(sizes, ops):
+        calls = [(op, *s, out) for s in sizes for op, out in forms if op in ops]
+        return [(c[1:4], x.kernel) for c, r in zip(calls, record(calls)) for x in r.launches if "quant" not in x.kernel]
+
+    wanted = {k for _, k in kernels(grid, ("product", "pair", "swiglu"))}
+    assert len(wanted) >= 30
+    seen = kernels([s[:3] for s in PRODUCTS], ("product",)) + kernels([s[:3] for s in PAIRS], ("pair", "swiglu"))
+    for kernel in sorted(wanted):
+        rows, cols, groups, places, past_caches = tile_of(kernel)
+        ends = {(-(-K // 128) % places, K % 128 != 0) for (M, N, K), k in seen
+                if k == kernel and -(-K // 128) >= groups and M % rows and (cols <= 64 or N % cols)}
+        assert any(half for _, half in ends), kernel
+        if not past_caches:  # the same kernel but for the kind of load
+            assert {e for e, _ in ends} == set(range(places)), (kernel, ends)
+            assert "direct" in kernel or any(k == kernel and M > 2 * rows and N > 2 * cols for (M, N, K), k in seen), kernel
