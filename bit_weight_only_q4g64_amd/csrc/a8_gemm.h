@@ -14,15 +14,18 @@
 //     conversion. Its products are exact, but it adds them eight at a time
 //     after aligning them to the largest, and drops what lies below 2^-13 of
 //     that product's power of two (measured: 2^16 + 2^3 is exact, 2^16 + 2^2
-//     gives 2^16 when the two share a run of 8, and is exact when they do
-//     not). On normal values the result is 1.4e-5 off (2-norm);
+//     gives 2^16 when the two share a run of 8 consecutive k; different runs
+//     and the accumulator are added in float32, in the 32 x 32 x 64 form too:
+//     2^16 + 2^-7 is exact). On normal values the result is 1.4e-5 off
+//     (2-norm);
 //   * the bf16 one, four chained steps of 16 x 16 x 32 on the codes converted
 //     to bf16, which holds every E4M3 value. Products are exact and the sums
 //     are float32: 1e-7 off.
 // A float32 result takes the second: the first would leave it with 16 bits. So
 // does an 8-bit result, whose scales are float32 (2.4e-5 off from the first).
-// A bf16 result takes the first: its own rounding (2^-9) is a hundred times
-// larger than what the instruction drops.
+// A bf16 result takes the first: its own rounding (at most 2^-8 of the value,
+// 1.7e-3 in the 2-norm) is a hundred times larger than what the instruction
+// drops.
 //
 // Weights are read in the layout pack_fp8b leaves: lane L of a wave owns, of a
 // 16-column tile and 128 k, the 32 bytes of column L % 16 at

@@ -8,7 +8,7 @@ import re
 import pytest
 
 import bit_weight_only_q4g64_amd as q4
-from tests.a8_shapes import PAIRS, PRODUCTS
+from tests.a8_shapes import BF16_KERNELS, PAIRS, PRODUCTS
 from tests.launch_record import available, record
 
 pytestmark = pytest.mark.skipif(not available, reason="needs the ROCm compilers")
@@ -84,3 +84,11 @@ def test_shapes_take_every_kernel_through_its_pipeline():
         if not past_caches:  # the same kernel but for the kind of load
             assert {e for e, _ in ends} == set(range(places)), (kernel, ends)
             assert "direct" in kernel or any(k == kernel and M > 2 * rows and N > 2 * cols for (M, N, K), k in seen), kernel
+
+
+def test_sizes_of_every_bfloat16_kernel():
+    def kernels(sizes):
+        return {x.kernel for r in record([("product", *s, "bf16") for s in sizes]) for x in r.launches}
+
+    grid = [(M, N, 1088) for M in (1, 17, 50, 100, 200, 400, 700, 1500, 3000, 8000) for N in (64, 256, 448, 1024, 1344, 2048, 4096, 8192)]
+    assert kernels(grid) == kernels(BF16_KERNELS) and len(kernels(BF16_KERNELS)) == len(BF16_KERNELS)
