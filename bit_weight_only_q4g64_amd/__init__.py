@@ -669,7 +669,12 @@ def _a8_stream(t: torch.Tensor) -> int:
     return _raw_stream(dev)
 
 
-def _a8_out_type(dtype) -> int:
+def _a8_out_type(dtype, default, y) -> int:
+    """The type of a new result; a given y keeps its own, which a given dtype has to be."""
+    if dtype is None:
+        dtype = default
+    elif y is not None and y.dtype != dtype:
+        raise ValueError("out_dtype is not y's type")
     code = _A8_TYPES.get(dtype)
     if code is None:
         raise ValueError("out_dtype must be bfloat16 or float32")
@@ -688,11 +693,12 @@ def quant_a8(x: torch.Tensor, out: Act8 | None = None) -> Act8:
 
 
 def rms_norm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: torch.Tensor | None = None,
-             residual_out: torch.Tensor | None = None, y: torch.Tensor | None = None, out_dtype=torch.bfloat16):
+             residual_out: torch.Tensor | None = None, y: torch.Tensor | None = None, out_dtype=None):
     """y = h / sqrt(mean(h^2) + eps) * gamma, h = x + residual rounded to the residual's type. x and residual are
-    bfloat16 or float32 [M][K], y of out_dtype. Returns y, or (y, h) with a residual; h goes to residual_out (which
-    may be residual itself) or a new tensor."""
-    r = (_bound or _binding()).norm(_a8_stream(x), x, gamma, eps, residual, residual_out, y, _a8_out_type(out_dtype))
+    bfloat16 or float32 [M][K]; y is too, a new one of out_dtype (bfloat16 if None). Returns y, or (y, h) with a
+    residual; h goes to residual_out (which may be residual itself) or a new tensor."""
+    t = _a8_out_type(out_dtype, torch.bfloat16, y)
+    r = (_bound or _binding()).norm(_a8_stream(x), x, gamma, eps, residual, residual_out, y, t)
     return r[0] if residual is None else r
 
 
@@ -709,11 +715,12 @@ def rms_norm_a8(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: torc
 
 
 def qmm_a8_fp8b(pa: torch.Tensor, pb: torch.Tensor | None, N: int, K: int, x: Act8, y: torch.Tensor | None = None,
-                out_dtype=torch.float32) -> torch.Tensor:
-    """y = A x of 8-bit rows, or silu(A x) * (B x), with block-FP8 weights packed by pack_fp8b. A float32 y is the sum
-    of exact products; a bfloat16 y comes from the 8-bit matrix instructions, which are up to twice as fast."""
-    data = x.data
-    return (_bound or _binding()).product(_a8_stream(data), pa, pb, N, K, data, x.scales, y, _a8_out_type(out_dtype))
+                out_dtype=None) -> torch.Tensor:
+    """y = A x of 8-bit rows, or silu(A x) * (B x), with block-FP8 weights packed by pack_fp8b; a new y is of out_dtype
+    (float32 if None). A float32 y is the sum of exact products; a bfloat16 y comes from the 8-bit matrix instructions,
+    which are up to twice as fast."""
+    t, data = _a8_out_type(out_dtype, torch.float32, y), x.data
+    return (_bound or _binding()).product(_a8_stream(data), pa, pb, N, K, data, x.scales, y, t)
 
 
 def a8_swiglu_work_bytes(M: int, N: int, K: int) -> int:
