@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sysconfig
 
 import torch
 
@@ -613,7 +614,7 @@ def qmv_qkv_rope(packed: torch.Tensor, K: int, x: torch.Tensor, pos: torch.Tenso
 # their marshalling is in C++ (csrc/a8_binding.cpp): a refused argument raises
 # ValueError, a call that the library refuses Q4Error, as above.
 
-BINDING_PATH = os.path.join(_HERE, "_a8.so")
+BINDING_PATH = os.path.join(_HERE, "_a8" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 _bound = None
 
@@ -624,7 +625,8 @@ def _binding():
     if _bound is None:
         lib()
         if not os.path.exists(BINDING_PATH):
-            raise RuntimeError(f"{BINDING_PATH} is not built; run `python -m bit_weight_only_q4g64_amd.build`")
+            raise RuntimeError(f"{BINDING_PATH} is not built; run `python -m bit_weight_only_q4g64_amd.build` "
+                               "(it needs Python's and torch's headers)")
         from . import _a8 as module
 
         module.setup(Q4Error)

@@ -5,11 +5,14 @@
 compiles the two translation units ``csrc/api.hip`` (the weight-only matmuls)
 and ``csrc/a8.hip`` (the 8-bit activation path) side by side and links them into
 ``bit_weight_only_q4g64_amd/libq4g64.so``, then compiles the C++ marshalling of
-the 8-bit calls (``csrc/a8_binding.cpp``, host code only) into ``_a8.so`` beside
-it. Strict IEEE float32: no fast-math and
-no floating-point contraction (every fused multiply-add in the kernels is an
-explicit fma), no packed-fp32 instructions, and matrix-core results kept in
-ordinary vector registers.
+the 8-bit calls (``csrc/a8_binding.cpp``, host code only) into an extension
+module of this interpreter beside it (``_a8.cpython-....so``). hipcc compiles
+both. The marshalling also needs Python's and torch's headers; where they are
+missing, the build warns and leaves it out, and only the 8-bit calls are
+unavailable. Strict IEEE float32: no fast-math and no floating-point
+contraction (every fused multiply-add in the kernels is an explicit fma), no
+packed-fp32 instructions, and matrix-core results kept in ordinary vector
+registers.
 """
 
 from __future__ import annotations
@@ -19,13 +22,15 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", name) for name in ("api.hip", "a8.hip")]
 OUT = os.path.join(HERE, "libq4g64.so")
 BINDING_SRC = os.path.join(HERE, "csrc", "a8_binding.cpp")
-BINDING_OUT = os.path.join(HERE, "_a8.so")
+BINDING_OUT = os.path.join(HERE, "_a8" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_HEADERS = ("Python.h", "ATen/ATen.h", "ATen/hip/EmptyTensor.h", "torch/csrc/autograd/python_variable.h")
 ARCH = "gfx950"
 
 FLAGS = [
@@ -82,22 +87,37 @@ def build(verbose: bool = False) -> str:
     return OUT
 
 
-def build_binding() -> str:
-    """Compile the C++ marshalling against this interpreter's torch, with its ABI, and return its path."""
+def binding_includes() -> list:
+    """Folders of the headers that the marshalling is compiled against: torch's and this interpreter's."""
     import torch
 
-    root = os.path.dirname(torch.__file__)
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    return [root, os.path.join(root, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"]]
+
+
+def build_binding() -> str | None:
+    """Compile the C++ marshalling against this interpreter's torch, with its ABI, and return its path; None (and a
+    warning) where the headers are missing. What was there before goes first: it is of another library."""
+    import torch
+
+    for old in (BINDING_OUT, os.path.join(os.path.dirname(BINDING_OUT), "_a8.so")):
+        if os.path.exists(old):
+            os.remove(old)
+    inc = binding_includes()
+    missing = [h for h in BINDING_HEADERS if not any(os.path.exists(os.path.join(d, h)) for d in inc)]
+    if missing:
+        warnings.warn(f"the 8-bit calls are left out: no {', '.join(missing)} in {', '.join(inc)}")
+        return None
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
-    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"], os.path.join(rocm, "include")]
-    libs = os.path.join(root, "lib")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING_OUT + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in inc), BINDING_SRC, "-o", tmp,
-           f"-L{HERE}", "-l:libq4g64.so", f"-L{libs}", "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    cmd = [hipcc(), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in (*inc, os.path.join(rocm, "include"))),
+           BINDING_SRC, "-o", tmp, f"-L{HERE}", "-l:libq4g64.so", f"-L{libs}", "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
+           "-lc10", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"g++ failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stderr}")
+        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stderr}")
     os.replace(tmp, BINDING_OUT)
     return BINDING_OUT
 
