@@ -10,18 +10,26 @@
 //
 // Operands. The activations of a group move from memory to LDS by
 // buffer-to-LDS DMA, PD + 1 groups ahead, and from there to registers one
-// row tile ahead; the weights go straight from memory to registers PD groups
-// ahead. Neither path could carry both: LDS gives 64 bytes a cycle, and so does
-// the path from memory.
+// row tile ahead: the workgroup's waves share them, and load them once. The
+// weights belong to one wave each and go straight from memory to registers PD
+// groups ahead. What comes from memory is the scarcer path: a compute unit
+// gets 64 bytes a cycle from its cache and 60 from L2, and over 200 from LDS
+// (measured with 8 waves, 16 bytes a lane).
 //
-// What bounds it. Many rows of bf16 results: the matrix cores at the clock that
-// the power limit leaves (1.8 GHz with real values, 2.4 with zeros): 8192 x 2048
-// x 8192 in 127 us, 2.1 PFLOP/s of 8-bit products. Exact results: the bf16
-// matrix steps, half of a wave's time, and the wait for weights that it can ask
-// for only one group ahead, because accumulators, converted operands and
-// products leave no more registers: SwiGLU to 8 bits of 8192 x 8192 x 2048 in
-// 500 us, 1.1 PFLOP/s. One row of workgroups: the weights from memory, 128 x
-// 65536 x 2048 in 34 us, 4.4 TB/s.
+// What bounds it. Many rows of bf16 results: 8192 x 2048 x 8192 takes 134-141
+// us with inputs that rotate through memory, 124-130 with one set of inputs,
+// 2.0-2.2 PFLOP/s of 8-bit products. The matrix cores are busy 53 % of the
+// cycles and the VALU issues 41 %: the 128 x 256 tile has no registers to fold
+// a product one late, so a wave's matrix steps and folds take turns, and the
+// one other wave of its SIMD does not fill the gaps. The clock is 1.9 GHz under
+// the power limit with real values, 2.4 with zeros (97 us, the same cycles).
+// Exact results: the bf16 matrix steps, half of a wave's time, and the wait for
+// weights that it can ask for only one group ahead, because accumulators,
+// converted operands and products leave no more registers: SwiGLU to 8 bits of
+// 8192 x 8192 x 2048 in 500-517 us, 1.1 PFLOP/s. (The pair with a float32
+// result is two registers short: two lane indexes lie in scratch memory from
+// before the loop until after it.) One row of workgroups: the weights from
+// memory, 128 x 65536 x 2048 in 33 us, 4.6 TB/s.
 //
 // Lane order. A lane of the instruction holds 32 bytes of k for row (column)
 // L % 32. Of piece j of a column (64 k) the packed weights hold, for q = 0..3,
