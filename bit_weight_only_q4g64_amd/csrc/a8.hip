@@ -299,15 +299,17 @@ bool pair_launch(const q4::GemmA8Args& a, hipStream_t s) {
 // first saves more than the second costs: 1.5 us and 4 TB/s on the GPU, and a
 // host that needs 9 us for the two launches (16 x 1024 x 8192: 13 us against
 // 52; 4 x 8192 x 2048: 9.3 against 14; 10 x 1152 x 64: 9.6 against 6).
-// Only while the one launch has at most two workgroups per compute unit: past
-// that the chip is full, the two estimates differ by less than their error
-// where K passes the fitted range, and the second launch would have to move
-// M x N float32 values (two launches / one, us: 5474 x 320 x 10944 of 258
-// workgroups 108 / 144, 1226 x 1600 x 10368 of 507 118 / 130; 4096 x 8192 x
-// 28672 of 4096 3429 / 3396, 8192 x 8192 x 20480 of 8192 4907 / 4856). So
-// `work` is at most 512 x 64 x 128 floats, and the quantizer's launch is far
-// inside its limit whenever the pair's has been enqueued.
-constexpr int64_t kSplitTiles = 512;
+// Only while the one launch has at most three workgroups per compute unit:
+// there the unfilled last round is worth up to 30 % (two launches / one, us:
+// 5474 x 320 x 10944 of 258 workgroups 108 / 144, 1226 x 1600 x 10368 of 507
+// 118 / 130, 12 x 67648 x 11008 of 529 243 / 318, 11008 x 320 x 10368 of 516
+// 193 / 206). Past that one launch is faster, by 1 to 40 % at 60 sizes, but the
+// estimates cross again where K passes the fitted range (4096 x 8192 x 28672 of
+// 4096 3429 / 3396, 8192 x 8192 x 20480 of 8192 4907 / 4856), and the second
+// launch would move M x N float32 values. So `work` is at most 768 x 64 x 128
+// floats, and the quantizer's launch is far inside its limit whenever the
+// pair's has been enqueued.
+constexpr int64_t kSplitTiles = 768;
 bool quant_splits(int64_t M, int64_t N, int64_t K) {
   M = rows16(M);
   const Tile& t = kPairQuant[best_tile(kPairQuant, M, N, K)];

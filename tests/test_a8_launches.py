@@ -32,14 +32,15 @@ def test_a_refused_call_launches_nothing():
 
 
 def test_scratch_memory_stays_small():
-    """M x N float32 values of scratch memory for few workgroups only, however long K is (512 of 64 x 128 at most)."""
+    """M x N float32 values of scratch memory for few workgroups only, however long K is (768 of 64 x 128 at most)."""
     need = q4.a8_swiglu_work_bytes
     for M, N, K in ((8192, 8192, 20480), (4096, 8192, 28672), (8192, 8192, 65536), (2**18, 2**17, 16384), (2048, 28672, 2**20)):
         assert need(M, N, K) == 0, (M, N, K)
     sizes = [(2**m + d, 2**n, k) for m in range(4, 21) for d in (0, 1) for n in range(6, 20) for k in (64, 1024, 8192, 16384, 20480, 2**16, 2**20)]
-    assert max(need(*s) for s in sizes) <= 512 * 64 * 128 * 4
+    assert max(need(*s) for s in sizes) <= 768 * 64 * 128 * 4
     # few workgroups still take the two launches
-    for M, N, K in ((16, 1024, 8192), (4, 8192, 2048), (5474, 320, 10944), (1226, 1600, 10368)):
+    for M, N, K in ((16, 1024, 8192), (4, 8192, 2048), (5474, 320, 10944), (1226, 1600, 10368),
+                    (12, 67648, 11008), (11008, 320, 10368)):
         assert need(M, N, K) == M * N * 4, (M, N, K)
 
 
