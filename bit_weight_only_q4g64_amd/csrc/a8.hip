@@ -303,12 +303,13 @@ bool pair_launch(const q4::GemmA8Args& a, hipStream_t s) {
 // there the unfilled last round is worth up to 30 % (two launches / one, us:
 // 5474 x 320 x 10944 of 258 workgroups 108 / 144, 1226 x 1600 x 10368 of 507
 // 118 / 130, 12 x 67648 x 11008 of 529 243 / 318, 11008 x 320 x 10368 of 516
-// 193 / 206). Past that one launch is faster, by 1 to 40 % at 60 sizes, but the
-// estimates cross again where K passes the fitted range (4096 x 8192 x 28672 of
-// 4096 3429 / 3396, 8192 x 8192 x 20480 of 8192 4907 / 4856), and the second
-// launch would move M x N float32 values. So `work` is at most 768 x 64 x 128
-// floats, and the quantizer's launch is far inside its limit whenever the
-// pair's has been enqueued.
+// 193 / 206). Past that one launch is up to 43 % faster, but for up to 32 rows
+// of short K (1 x 131072 x 2048 83 / 97), where the estimates keep to it too;
+// they cross again where K passes the fitted range (4096 x 8192 x 28672 of 4096
+// 3429 / 3396, 8192 x 8192 x 20480 of 8192 4907 / 4856), and the second launch
+// would move M x N float32 values. So `work` is at most 768 x 64 x 128 floats,
+// and the quantizer's launch is far inside its limit whenever the pair's has
+// been enqueued.
 constexpr int64_t kSplitTiles = 768;
 bool quant_splits(int64_t M, int64_t N, int64_t K) {
   M = rows16(M);

@@ -119,11 +119,12 @@ __device__ __forceinline__ void a8_store4(const GemmA8Args& a, int64_t m, int n,
 // x 2048 22.7 us, 5.9 TB/s. A small matrix is a launch (2.2 us), one trip to
 // memory and the join: 1 x 2048 x 2048 3.3 us; 16 x 2048 x 8192 7.7 us, on half
 // the compute units (splitting K over workgroups too would take a second
-// launch, or three round trips to hand the parts over). More waves per workgroup or loads further ahead are slower there
-// (8 waves, 2 groups ahead; 16 waves, 2 ahead; 8 waves, 4 ahead): 8.4, 8.7 and
-// 9.5 us with weights from memory, 4 x 65536 x 2048 22.7, 36 and 28 us. The
-// kernels of more rows have too few registers for two groups (200 x 2048 x 8192
-// float32 on 32 x 32 24 us, with two 48 us).
+// launch, or three round trips to hand the parts over). More waves per
+// workgroup or loads further ahead are slower there (8 waves, 2 groups ahead;
+// 16 waves, 2 ahead; 8 waves, 4 ahead): 8.4, 8.7 and 9.5 us with weights from
+// memory, 4 x 65536 x 2048 22.7, 36 and 28 us. The kernels of more rows have
+// too few registers for two groups (200 x 2048 x 8192 float32 on 32 x 32 24 us,
+// with two 48 us).
 template <bool EXACT_, int MT_, int NT_, bool SW_, int NW_, int KW_, int D_>
 struct DirectA8 {
   static constexpr int MT = MT_, NT = NT_, NW = NW_, KW = KW_, D = D_;

@@ -440,9 +440,8 @@ float qmv_window_cost(const float* us, int R);
  * scales' product sx * sw is a float32 too: where it overflows, the group's
  * part of the row is infinite or NaN.)
  * The norm adds squares in float32, or in float64 where a row's would
- * leave float32, so every row of finite values has its norm; a row of zeros
- * with eps = 0 gives NaN, and one with an infinity NaN there and zeros
- * elsewhere.
+ * leave float32, so every row of finite h has its norm; a row of zeros with
+ * eps = 0 gives NaN, and one with an infinity NaN there and zeros elsewhere.
  *
  * Float32 and a8 results are sums of exact products, added in float32. A
  * Q4_BF16 product comes from the 8-bit matrix instructions, up to twice as

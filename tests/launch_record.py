@@ -2,11 +2,12 @@
 of a8.hip, compiled host-only and linked against a recorder in the HIP
 runtime's place (tests/host/launch_record.cpp)."""
 
+import atexit
 import functools
-import hashlib
 import os
 import pathlib
 import re
+import shutil
 import subprocess
 import tempfile
 from typing import NamedTuple
@@ -34,29 +35,20 @@ class Call(NamedTuple):
 
 @functools.lru_cache(None)
 def _program() -> pathlib.Path:
-    sources = [*sorted(CSRC.glob("*.h")), CSRC / "a8.hip", ROOT / "include" / "q4g64.h", DRIVER]
-    key = hashlib.sha256(b"".join(s.read_bytes() for s in sources)).hexdigest()[:16]
-    exe = pathlib.Path(tempfile.gettempdir()) / f"launch_record_{os.getuid()}_{key}"
-    if exe.exists():
-        return exe
-    with tempfile.TemporaryDirectory() as d:
-        tmp = pathlib.Path(d)
-        (tmp / "empty.hipfb").write_bytes(b"")  # no device code
-        for cmd in (
-            [HIPCC, "--offload-arch=gfx950", "--cuda-host-only", "-O1", "-std=c++17", "-Xclang", "-fcuda-include-gpubinary",
-             "-Xclang", tmp / "empty.hipfb", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-             "-I", ROOT / "include", "-c", CSRC / "a8.hip", "-o", tmp / "a8.o"],
-            [CLANG, "-O1", "-std=c++17", "-D__HIP_PLATFORM_AMD__", "-I", ROOT / "include", "-I", "/opt/rocm/include", DRIVER, tmp / "a8.o",
-             "-o", tmp / "exe"],
-        ):
-            r = subprocess.run([str(c) for c in cmd], capture_output=True, text=True, timeout=600)
-            assert r.returncode == 0, r.stderr[-4000:]
-        fd, part = tempfile.mkstemp(dir=exe.parent)
-        os.close(fd)
-        pathlib.Path(part).write_bytes((tmp / "exe").read_bytes())
-        os.chmod(part, 0o755)
-        os.replace(part, exe)
-    return exe
+    """The recorder, built once per process."""
+    tmp = pathlib.Path(tempfile.mkdtemp(prefix="launch_record_"))
+    atexit.register(shutil.rmtree, tmp, True)
+    (tmp / "empty.hipfb").write_bytes(b"")  # no device code
+    for cmd in (
+        [HIPCC, "--offload-arch=gfx950", "--cuda-host-only", "-O1", "-std=c++17", "-Xclang", "-fcuda-include-gpubinary",
+         "-Xclang", tmp / "empty.hipfb", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+         "-I", ROOT / "include", "-c", CSRC / "a8.hip", "-o", tmp / "a8.o"],
+        [CLANG, "-O1", "-std=c++17", "-D__HIP_PLATFORM_AMD__", "-I", ROOT / "include", "-I", "/opt/rocm/include", DRIVER, tmp / "a8.o",
+         "-o", tmp / "launch_record"],
+    ):
+        r = subprocess.run([str(c) for c in cmd], capture_output=True, text=True, timeout=600)
+        assert r.returncode == 0, r.stderr[-4000:]
+    return tmp / "launch_record"
 
 
 def record(calls) -> list:
